@@ -41,6 +41,18 @@ def causal_conv(u, w, bias=None):
     return y[:, :L, 0]
 
 
+def last_inputs(u, taps, lengths=None):
+    """The last taps - 1 rows of u [B, L, D] before each batch row's end, zeros before its beginning.
+
+    lengths counts as the recurrence takes it: clamped to [0, L].
+    """
+    B, L, _ = u.shape
+    n = torch.full((B,), L, device=u.device) if lengths is None else lengths.long().clamp(0, L)
+    at = n[:, None] + torch.arange(1 - taps, 0, device=u.device)
+    rows = u[torch.arange(B, device=u.device)[:, None], at.clamp_min(0)]
+    return torch.where((at >= 0)[..., None], rows, 0)
+
+
 class State(NamedTuple):
     conv: torch.Tensor   # [B, taps - 1, D]: the last inputs of the convolution
     h: torch.Tensor      # [B, D], fp32
@@ -83,11 +95,7 @@ class RecurrentLayer:
         r, i, g = gates[..., :D], gates[..., D:2 * D], gates[..., 2 * D:]
         h, last = seq.glr_fwd(causal_conv(u, self.conv_w, self.conv_b), r, i, self.lam, lengths=lengths)
         out = self._leave(h.view(B * L, D), g.reshape(B * L, D))
-        # the last taps - 1 inputs before each row's end, zeros before its beginning
-        n = torch.full((B,), L, device=x.device) if lengths is None else lengths.long()
-        at = n[:, None] + torch.arange(1 - taps, 0, device=x.device)
-        tail = u[torch.arange(B, device=x.device)[:, None], at.clamp_min(0)]
-        return out.view(B, L, E), total.view(B, L, E), State(torch.where((at >= 0)[..., None], tail, 0), last)
+        return out.view(B, L, E), total.view(B, L, E), State(last_inputs(u, taps, lengths), last)
 
     def token(self, x, residual, state: State):
         """x, residual [B, E] and the state, which moves on in place: (out, total)."""

@@ -100,6 +100,19 @@ def test_tokens_go_on_from_a_prompt():
         assert (np.abs(f64(s.h) - f["h_last"]) <= off["h_last"] + f["tol_h"]).all()
 
 
+def test_prompt_clamps_lengths():
+    """Lengths below 0 and past L are 0 and L, for the convolution's window as for the recurrence."""
+    l = layer()
+    B, L, E = 4, 70, 48
+    g = torch.Generator(device="cuda").manual_seed(8)
+    x, res = (torch.randn(B, L, E, device="cuda", generator=g) for _ in range(2))
+    n = torch.tensor([-5, L + 1, 2 ** 31 - 1, 7], dtype=torch.int32, device="cuda")
+    out, total, state = l.prompt(x, res, lengths=n)
+    want = l.prompt(x, res, lengths=n.clamp(0, L))
+    assert torch.equal(out, want[0]) and torch.equal(total, want[1])
+    assert torch.equal(state.conv, want[2].conv) and torch.equal(state.h, want[2].h)
+
+
 def test_mixer_gradients():
     """Each step's gradients from what the step before it gave, in fp64."""
     B, L, D, taps = 2, 90, 24, 4
