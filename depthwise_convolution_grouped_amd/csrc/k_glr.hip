@@ -683,23 +683,23 @@ template <typename T, bool FAR, bool AHEAD> __global__ __launch_bounds__(kLanes 
     }
 }
 
-// dlambda from the blocks' sums of w, added in order: 32 threads a channel
+// dlambda of n channels from the blocks' sums of w, rows of D, added in order: 32 threads a channel
 // take every 32nd row each, then one joins them.  4.6 us for 16 rows of 2048, a
 // launch's time; the last block of bwd_k to end doing it instead gains nothing
 // (1 x 16384 x 2048 147 us either way).
 __global__ __launch_bounds__(1024) void dlambda_k(const float *part, const float *lambda, float *dlambda, long long rows,
-                                                  int D)
+                                                  int D, int n)
 {
     __shared__ float lds[32][33];
     const int lane = threadIdx.x % 32, sub = threadIdx.x / 32, ch = blockIdx.x * 32 + lane;
     float t = 0.0f;
-    if (ch < D) {
+    if (ch < n) {
 #pragma unroll 4
         for (long long k = sub; k < rows; k += 32) t += part[k * D + ch];
     }
     lds[sub][lane] = t;
     __syncthreads();
-    if (sub || ch >= D) return;
+    if (sub || ch >= n) return;
     t = 0.0f;
     for (int j = 0; j < 32; ++j) t += lds[j][lane];
     const float l = lambda[ch], sp = softplus(l), e = expf(-fabsf(l));
@@ -787,32 +787,91 @@ Params params(const gconv_glr_desc &d, const Shape &s)
     return p;
 }
 
+// A launch's grid times its block stays below 2^32, so what may need more goes
+// in ranges: batch rows (whole rows, n of them from b on), and of split rows the
+// blocks, which take their chunks' numbers from counters and go on where the
+// launch before stopped.
+Params rows_from(Params p, long long b, long long n, long long e)
+{
+    auto move = [&](auto &t, const long long *stride) {
+        if (t) t = (std::remove_reference_t<decltype(t)>)((char *)t + b * stride[0] * e);
+    };
+    move(p.x, p.sx), move(p.r, p.sr), move(p.i, p.si), move(p.y, p.sy), move(p.dy, p.sy);
+    move(p.dx, p.sdx), move(p.dr, p.sdr), move(p.di, p.sdi);
+    if (p.lengths) p.lengths += b;
+    if (p.h0) p.h0 += b * p.D;
+    if (p.h_last) p.h_last += b * p.D;
+    if (p.states) p.states += b * p.nspan * p.D;
+    if (p.part) p.part += b * p.D;
+    p.B = (int)n;
+    return p;
+}
+
+// f(Params of a range, its grid) for all batch rows, the time axis whole.
+template <typename F> hipError_t whole_rows(const gconv_glr_desc &d, const Params &p, unsigned block, long long e, F &&f)
+{
+    const long long most = most_blocks(block) / p.tiles;
+    if (d.B <= most) return f(p, (unsigned)(p.tiles * d.B));
+    for (long long b = 0; b < d.B; b += most) {
+        const long long n = d.B - b < most ? d.B - b : most;
+        const hipError_t r = f(rows_from(p, b, n, e), (unsigned)(p.tiles * n));
+        if (r != hipSuccess) return r;
+    }
+    return hipSuccess;
+}
+
 template <typename T, bool FAR> hipError_t fwd_t(const gconv_glr_desc &d, const Shape &sh, Params p, void *ws, hipStream_t st)
 {
-    const unsigned grid = (unsigned)((long long)p.tiles * p.nchunk * d.B), block = kLanes * kRuns;
-    if (d.L <= kSerial) {
-        const Few f{p.x, p.r, p.i, p.y, p.lambda, p.h0, p.lengths, p.h_last, p.states,
-                    {p.sx[0], p.sx[1]}, {p.sr[0], p.sr[1]}, {p.si[0], p.si[1]}, {p.sy[0], p.sy[1]},
-                    p.L, p.D, p.nspan, p.tiles, p.c};
-        return start(fwd_serial_k<T>, grid, 64, 0, st, f);
-    }
-    if (p.nchunk == 1) return start(fwd_k<T, false, FAR>, grid, block, 0, st, p);
-    const long long n = (long long)words(d, sh);
+    constexpr unsigned block = kLanes * kRuns;
+    if (d.L <= kSerial)
+        return whole_rows(d, p, 64, sizeof(T), [&](const Params &q, unsigned grid) {
+            const Few f{q.x, q.r, q.i, q.y, q.lambda, q.h0, q.lengths, q.h_last, q.states,
+                        {q.sx[0], q.sx[1]}, {q.sr[0], q.sr[1]}, {q.si[0], q.si[1]}, {q.sy[0], q.sy[1]},
+                        q.L, q.D, q.nspan, q.tiles, q.c};
+            return start(fwd_serial_k<T>, grid, 64, 0, st, f);
+        });
+    if (p.nchunk == 1)
+        return whole_rows(d, p, block, sizeof(T),
+                          [&](const Params &q, unsigned grid) { return start(fwd_k<T, false, FAR>, grid, block, 0, st, q); });
+    const long long words_all = (long long)words(d, sh), words_most = most_blocks(256) * 256;
     p.ticket = (unsigned *)ws;
     p.pairs = (unsigned long long *)((char *)ws + tickets(d, sh));
     p.heads = p.pairs + (size_t)d.B * sh.nchunk * d.D;
-    const hipError_t e = start(clear_k, (unsigned)up(n, 256), 256, 0, st, p.ticket, (int)(p.tiles * d.B), p.pairs, n);
-    return e != hipSuccess ? e : start(fwd_k<T, true, FAR>, grid, block, 0, st, p);
+    const long long chains = p.tiles * d.B;
+    hipError_t e = hipSuccess;
+    for (long long k = 0; k < words_all && e == hipSuccess; k += words_most) {
+        const long long n = words_all - k < words_most ? words_all - k : words_most;
+        e = start(clear_k, (unsigned)up(n, 256), 256, 0, st, p.ticket, (int)chains, p.pairs + k, n);
+    }
+    const long long all = chains * p.nchunk, most = most_blocks(block) / chains * chains;
+    for (long long k = 0; k < all && e == hipSuccess; k += most)
+        e = start(fwd_k<T, true, FAR>, (unsigned)(all - k < most ? all - k : most), block, 0, st, p);
+    return e;
 }
 
-template <typename T, bool FAR> hipError_t bwd_t(const gconv_glr_desc &d, Params p, hipStream_t st)
+template <typename T, bool FAR> hipError_t bwd_t(const gconv_glr_desc &d, const Params &p, hipStream_t st)
 {
-    const unsigned row = (unsigned)(p.tiles * d.B), block = kLanes * kRuns;
+    constexpr unsigned block = kLanes * kRuns;
     if (p.nchunk == 1)
-        return row <= kAhead ? start(bwd_k<T, FAR, true>, row, block, 0, st, p)
-                             : start(bwd_k<T, FAR, false>, row, block, 0, st, p);
+        return whole_rows(d, p, block, sizeof(T), [&](const Params &q, unsigned grid) {
+            return p.tiles * d.B <= kAhead ? start(bwd_k<T, FAR, true>, grid, block, 0, st, q)
+                                           : start(bwd_k<T, FAR, false>, grid, block, 0, st, q);
+        });
+    const unsigned row = (unsigned)(p.tiles * d.B);   // below kBwdSplit, with about kBwdBlocks blocks in all
     const hipError_t e = start(bwd_reduce_k<T, FAR>, row * (p.nchunk - 1), block, 0, st, p);
     return e != hipSuccess ? e : start(bwd_k<T, FAR, false>, row * p.nchunk, block, 0, st, p);
+}
+
+// No step at all: the state, or its gradient, to where it goes.
+hipError_t pass(const float *from, float *to, long long n, hipStream_t s)
+{
+    const long long most = most_blocks(256) * 256;
+    hipError_t e = hipSuccess;
+    for (long long k = 0; k < n && e == hipSuccess; k += most) {
+        const long long m = n - k < most ? n - k : most;
+        e = start(pass_k, (unsigned)up(m, 256), 256, 0, s, from ? from + k : nullptr, to + k, m);
+    }
+    return e;
 }
 
 // f of a value of the element type, and of whether a block's offsets, in
@@ -830,13 +889,11 @@ template <typename F> hipError_t by_type(const gconv_glr_desc &d, bool backward,
 
 }  // namespace
 
-// Every launch's grid stays in an int, the one that clears the pairs too.
-bool fits(const gconv_glr_desc &d)
+// One batch row's channels are one launch: blocks of kLanes * kRuns threads hold
+// fewer than 2^29 of them, so that a channel's byte offset stays below 2^31.
+bool fits(const gconv_glr_desc &d, bool backward)
 {
-    const Shape f = fwd_shape(d), b = bwd_shape(d);
-    const double rows = (double)f.tiles * (double)d.B;
-    return rows * f.nchunk <= (double)kMaxGrid && rows * b.nchunk <= (double)kMaxGrid &&
-           (double)words(d, f) <= 256.0 * kMaxGrid && (double)d.B * (double)d.D <= 256.0 * kMaxGrid;
+    return (!backward && d.L <= kSerial) || up(d.D, kLanes) <= most_blocks(kLanes * kRuns);
 }
 
 size_t fwd_workspace(const gconv_glr_desc &d) { return d.B == 0 || d.L <= kSerial ? 0 : fwd_bytes(d, fwd_shape(d)); }
@@ -853,9 +910,8 @@ size_t bwd_min_workspace(const gconv_glr_desc &d) { return d.B == 0 || d.L == 0 
 hipError_t fwd(const gconv_glr_desc &d, const Fwd &a, size_t ws_bytes, hipStream_t s)
 {
     if (d.L == 0) {
-        const long long n = d.B * d.D;
         if (!a.h_last || a.h_last == a.h0) return hipSuccess;
-        return start(pass_k, (unsigned)up(n, 256), 256, 0, s, a.h0, a.h_last, n);
+        return pass(a.h0, a.h_last, d.B * d.D, s);
     }
     Shape sh = fwd_shape(d);
     if (d.L <= kSerial || ws_bytes < fwd_bytes(d, sh) || !on(a.ws, 8)) sh = whole(d);
@@ -878,8 +934,7 @@ hipError_t bwd(const gconv_glr_desc &d, const Bwd &a, size_t ws_bytes, hipStream
     const float *part = nullptr;
     long long rows = 0;
     if (d.B > 0 && d.L == 0) {
-        const long long n = d.B * d.D;
-        if (a.dh0 && a.dh0 != a.dh_last) e = start(pass_k, (unsigned)up(n, 256), 256, 0, s, a.dh_last, a.dh0, n);
+        if (a.dh0 && a.dh0 != a.dh_last) e = pass(a.dh_last, a.dh0, d.B * d.D, s);
     } else if (d.B > 0) {
         Shape sh = bwd_shape(d);
         if (ws_bytes < bwd_pairs(d, sh) + bwd_parts(d, sh) || !on(a.ws, 8)) sh = whole(d);
@@ -902,8 +957,13 @@ hipError_t bwd(const gconv_glr_desc &d, const Bwd &a, size_t ws_bytes, hipStream
         rows = d.B * sh.nchunk;
         e = by_type(d, true, [&](auto t, auto far) { return bwd_t<decltype(t), decltype(far)::value>(d, p, s); });
     }
-    if (e != hipSuccess) return e;
-    return start(dlambda_k, (unsigned)up(d.D, 32), 1024, 0, s, part, a.lambda, a.dlambda, rows, (int)d.D);
+    const long long most = most_blocks(1024) * 32;
+    for (long long k = 0; k < d.D && e == hipSuccess; k += most) {
+        const long long n = d.D - k < most ? d.D - k : most;
+        e = start(dlambda_k, (unsigned)up(n, 32), 1024, 0, s, part ? part + k : nullptr, a.lambda + k, a.dlambda + k, rows,
+                  (int)d.D, (int)n);
+    }
+    return e;
 }
 
 }  // namespace glr

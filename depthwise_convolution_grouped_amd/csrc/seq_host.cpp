@@ -54,7 +54,7 @@ int check(const gconv_glr_desc *d, bool backward)
     } else if (!write_ok(d->y_stride, d->B, d->L, d->D)) {
         return GCONV_ERR_BAD_DESC;
     }
-    return glr::fits(*d) ? GCONV_OK : GCONV_ERR_TOO_LARGE;
+    return glr::fits(*d, backward) ? GCONV_OK : GCONV_ERR_TOO_LARGE;
 }
 
 int check(const gconv_q8_desc *d, const void *x, const void *residual, const void *weight, const void *q,

@@ -23,6 +23,8 @@ hipError_t start(void (*k)(KP...), unsigned grid, unsigned block, unsigned lds, 
 }
 
 constexpr long long kMaxGrid = 0x7fffffffll;   // workgroups in one launch
+// and work-items: a runtime refuses a grid whose blocks hold 2^32 or more
+constexpr long long most_blocks(unsigned block) { return 0xffffffffll / block; }
 
 inline bool on(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 inline long long up(long long a, long long b) { return (a + b - 1) / b; }
@@ -49,7 +51,7 @@ struct Bwd {
 size_t fwd_workspace(const gconv_glr_desc &d);
 size_t bwd_workspace(const gconv_glr_desc &d);
 size_t bwd_min_workspace(const gconv_glr_desc &d);
-bool fits(const gconv_glr_desc &d);
+bool fits(const gconv_glr_desc &d, bool backward);
 hipError_t fwd(const gconv_glr_desc &d, const Fwd &a, size_t ws_bytes, hipStream_t s);
 hipError_t bwd(const gconv_glr_desc &d, const Bwd &a, size_t ws_bytes, hipStream_t s);
 }  // namespace glr

@@ -359,7 +359,8 @@ int gconv_bwd_weight_noalloc(const gconv_desc *d, const void *x, const void *dy,
 typedef struct gconv_glr_desc {
     int32_t dtype;              /* gconv_dtype of x, r, i, y, dy, dx, dr, di */
     float c;                    /* finite, > 0 */
-    int64_t B, L, D;            /* B, L >= 0, D >= 1, each at most 2^31 - 1024 */
+    int64_t B, L, D;            /* B, L >= 0, D >= 1, each at most 2^31 - 1024; D at most
+                                   2^29 - 64 where L > 8 and in the backward call */
     int64_t x_stride[2], r_stride[2], i_stride[2];  /* batch, time; >= 0 (0 repeats a row) */
     int64_t y_stride[2];        /* y; dy in the backward call (where 0 is taken too) */
     int64_t dx_stride[2], dr_stride[2], di_stride[2]; /* backward call only */

@@ -332,6 +332,52 @@ def test_recurrence_offsets_past_32_bits():
     assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
+@pytest.mark.parametrize("B,L", [((1 << 26) + 1, 1), ((1 << 23) + 1, 9)])
+def test_recurrence_more_rows_than_a_launch_holds(B, L):
+    """2^32 work-items and more: rows of one channel that repeat ten, all of them checked."""
+    k = Case(10, L, 1, "bf16", lengths=[L, 0, 1, L, L, 5 % (L + 1), L, L - 1, L, L])
+    want = seq.glr_fwd(*k.args, h0=k.h0, lengths=k.n, save=True)
+    back = seq.glr_bwd(k.dy, *k.args, want[2], lengths=k.n, dh_last=k.dh)
+    at = torch.arange(B, device="cuda") % 10
+
+    def many(t):
+        return t.index_select(0, at)
+
+    x, r, i, n = many(k.x), many(k.r), many(k.i), many(k.n)
+    got = seq.glr_fwd(x, r, i, k.lam, h0=many(k.h0), lengths=n, save=True)
+    for a, b in zip(got, want):
+        assert torch.equal(a, many(b))
+    grads = seq.glr_bwd(many(k.dy), x, r, i, k.lam, got[2], lengths=n, dh_last=many(k.dh))
+    for a, b in zip(grads[:3] + grads[4:], back[:3] + back[4:]):
+        assert torch.equal(a, many(b))
+    # each row's share is the same fp32 number; B / 32 of them are added one after the other
+    shares = [seq.glr_bwd(k.dy[j:j + 1], x[j:j + 1], r[j:j + 1], i[j:j + 1], k.lam, want[2][j:j + 1],
+                          lengths=k.n[j:j + 1], dh_last=k.dh[j:j + 1])[3].double() for j in range(10)]
+    count = torch.bincount(at[:B], minlength=10).double()
+    total, mag = (float(sum(c * v for c, v in zip(count, s))) for s in (shares, [v.abs() for v in shares]))
+    assert abs(float(grads[3]) - total) <= (B / 32 + 64) * ref.U * mag
+
+
+def test_recurrence_more_chunks_than_a_launch_holds():
+    """A row of 2^30 and some steps, 2^23 and some chunks: constant inputs, so that the state settles.
+
+    Where it has, each of the settled fp32 states is within (6 + 32 |log a|) U + 66 U over 1 - a of the formula's."""
+    L, near_end = (1 << 30) + 1000, 5000
+    one = [torch.tensor(v).bfloat16().view(1, 1, 1).cuda() for v in (1.5, 2.0, 1.0)]
+    lam, h0 = torch.zeros(1, device="cuda"), torch.full((1, 1), 3.0, device="cuda")
+    y, last = seq.glr_fwd(*(v.expand(1, L, 1) for v in one), lam, h0=h0)
+    head, _ = seq.glr_fwd(*(v.expand(1, near_end, 1) for v in one), lam, h0=h0)
+    assert torch.equal(y[:, :near_end], head)
+    la = -8 * np.log(2) / (1 + np.exp(-2.0))
+    a = np.exp(la)
+    want = np.sqrt(1 - a * a) / (1 - a) * 1.5 / (1 + np.exp(-1.0))
+    tol = (72 + 32 * abs(la)) * ref.U / (1 - a) * want
+    assert abs(float(last) - want) <= tol
+    ends = y[0, 200:, 0].aminmax()
+    half = torch.finfo(torch.bfloat16).eps / 2 * want
+    assert abs(float(ends[0]) - want) <= tol + half and abs(float(ends[1]) - want) <= tol + half
+
+
 def test_recurrence_gradient_against_differences():
     """The fp32 forward's own central differences along random directions.
 

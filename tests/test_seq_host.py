@@ -72,6 +72,19 @@ def test_extents_leave_room_for_a_block(extent, status):
         G.GCONV_ERR_NULL_PTR if status == G.GCONV_OK else status)
 
 
+@pytest.mark.parametrize("L,D,forward,backward", [
+    (9, (1 << 29) - 64, G.GCONV_OK, G.GCONV_OK), (9, (1 << 29) - 63, G.GCONV_ERR_TOO_LARGE, G.GCONV_ERR_TOO_LARGE),
+    (9, (1 << 30) + 64, G.GCONV_ERR_TOO_LARGE, G.GCONV_ERR_TOO_LARGE),
+    (8, (1 << 31) - 1024, G.GCONV_OK, G.GCONV_ERR_TOO_LARGE)])
+def test_channels_of_a_row_fit_a_launch(L, D, forward, backward):
+    """A launch holds fewer than 2^32 work-items, 8 for each channel but in the kernel of up to eight steps; the
+    channels' byte offsets, which are 32-bit there, do not wrap below that."""
+    n = ctypes.c_size_t()
+    d = glr_desc(B=1, L=L, D=D, dtype=G.GCONV_F32, **{k: (0, D) for k in ("x", "r", "i", "y", "dx", "dr", "di")})
+    assert G.lib().gconv_glr_fwd_workspace(ctypes.byref(d), ctypes.byref(n)) == forward
+    assert G.lib().gconv_glr_bwd_workspace(ctypes.byref(d), ctypes.byref(n), None) == backward
+
+
 def test_recurrence_takes_time_major_and_repeated_rows():
     n = ctypes.c_size_t()
     for kw in (dict(y=(6, 12)), dict(x=(0, 6)), dict(x=(60, 0)), dict(B=0), dict(L=0), dict(y=(100, 7))):
