@@ -196,15 +196,29 @@ template <typename T, bool NORM> __global__ __launch_bounds__(1024) void long_k(
     }
 }
 
+// A block a row, in as many launches as their work-items' limit asks for.
+template <typename T> hipError_t rows(void (*k)(Params), unsigned block, Params p, long long M, hipStream_t s)
+{
+    const long long most = most_blocks(block);
+    for (;; M -= most) {
+        const hipError_t e = start(k, (unsigned)(M < most ? M : most), block, 0, s, p);
+        if (e != hipSuccess || M <= most) return e;
+        p.x = (const T *)p.x + most * p.sx;
+        if (p.res) p.res = (const T *)p.res + most * p.sr;
+        if (p.sum) p.sum = (T *)p.sum + most * p.ss;
+        p.q += most * p.sq;
+        p.scale += most;
+    }
+}
+
 template <typename T, bool NORM, bool ALIGNED> hipError_t launch(const Params &p, long long M, hipStream_t s)
 {
-    const unsigned g = (unsigned)M;
-    if (p.D <= 512) return start(held_k<T, 64, 1, NORM, ALIGNED>, g, 64, 0, s, p);
-    if (p.D <= 2048) return start(held_k<T, 256, 1, NORM, ALIGNED>, g, 256, 0, s, p);
-    if (p.D <= 4096) return start(held_k<T, 256, 2, NORM, ALIGNED>, g, 256, 0, s, p);
-    if (p.D <= 8192) return start(held_k<T, 256, 4, NORM, ALIGNED>, g, 256, 0, s, p);
-    if (p.D <= 16384) return start(held_k<T, 512, 4, NORM, ALIGNED>, g, 512, 0, s, p);
-    return start(long_k<T, NORM>, g, 1024, 0, s, p);
+    if (p.D <= 512) return rows<T>(held_k<T, 64, 1, NORM, ALIGNED>, 64, p, M, s);
+    if (p.D <= 2048) return rows<T>(held_k<T, 256, 1, NORM, ALIGNED>, 256, p, M, s);
+    if (p.D <= 4096) return rows<T>(held_k<T, 256, 2, NORM, ALIGNED>, 256, p, M, s);
+    if (p.D <= 8192) return rows<T>(held_k<T, 256, 4, NORM, ALIGNED>, 256, p, M, s);
+    if (p.D <= 16384) return rows<T>(held_k<T, 512, 4, NORM, ALIGNED>, 512, p, M, s);
+    return rows<T>(long_k<T, NORM>, 1024, p, M, s);
 }
 
 template <typename T> hipError_t launch(const Params &p, long long M, bool aligned, hipStream_t s)

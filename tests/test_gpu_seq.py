@@ -338,10 +338,9 @@ def test_recurrence_more_rows_than_a_launch_holds(B, L):
     k = Case(10, L, 1, "bf16", lengths=[L, 0, 1, L, L, 5 % (L + 1), L, L - 1, L, L])
     want = seq.glr_fwd(*k.args, h0=k.h0, lengths=k.n, save=True)
     back = seq.glr_bwd(k.dy, *k.args, want[2], lengths=k.n, dh_last=k.dh)
-    at = torch.arange(B, device="cuda") % 10
 
     def many(t):
-        return t.index_select(0, at)
+        return t.repeat((B // 10 + 1,) + (1,) * (t.dim() - 1))[:B]
 
     x, r, i, n = many(k.x), many(k.r), many(k.i), many(k.n)
     got = seq.glr_fwd(x, r, i, k.lam, h0=many(k.h0), lengths=n, save=True)
@@ -353,7 +352,7 @@ def test_recurrence_more_rows_than_a_launch_holds(B, L):
     # each row's share is the same fp32 number; B / 32 of them are added one after the other
     shares = [seq.glr_bwd(k.dy[j:j + 1], x[j:j + 1], r[j:j + 1], i[j:j + 1], k.lam, want[2][j:j + 1],
                           lengths=k.n[j:j + 1], dh_last=k.dh[j:j + 1])[3].double() for j in range(10)]
-    count = torch.bincount(at[:B], minlength=10).double()
+    count = [len(range(j, B, 10)) for j in range(10)]
     total, mag = (float(sum(c * v for c, v in zip(count, s))) for s in (shares, [v.abs() for v in shares]))
     assert abs(float(grads[3]) - total) <= (B / 32 + 64) * ref.U * mag
 
@@ -512,6 +511,24 @@ def test_rows_strides_and_in_place(D):
     assert (q[:, :8] == 99).all() and (q[:, D + 8:] == 99).all()
     one = seq.quant_q8(x[:1].expand(4, D))     # one row, four times
     assert torch.equal(one[0], seq.quant_q8(x[:1])[0].expand(4, D))
+
+
+@pytest.mark.parametrize("D,threads", [(8, 64), (520, 256)])
+def test_rows_more_than_a_launch_holds(D, threads):
+    """2^32 work-items and more, a block a row: rows that repeat ten, all of them checked."""
+    M = (1 << 32) // threads + 3
+    x, res = torch.randn(10, D, device="cuda").bfloat16(), torch.randn(10, D, device="cuda").bfloat16()
+    w = torch.rand(D, device="cuda") + 0.5
+    # a plain, a normed and a summed row, the first ones read over and over with a stride of 0
+    q, scale = seq.quant_q8(x[:1].expand(M, D))
+    want = seq.quant_q8(x[:1])
+    assert (q == want[0]).all() and (scale == want[1]).all()
+    del q, scale
+    got = seq.rmsnorm_q8(x.repeat(M // 10 + 1, 1)[:M], w, residual=res[:1].expand(M, D))
+    want = seq.rmsnorm_q8(x, w, residual=res[:1].expand(10, D))
+    for j in range(10):
+        for a, b in zip(got, want):
+            assert (a[j::10] == b[j]).all()
 
 
 @pytest.mark.parametrize("D", [64, 65, 9000])
