@@ -648,6 +648,7 @@ int lying_best(const Params &p)
 }
 bool pack_pays(const Params &p)
 {
+    if (((double)p.M + p.N) * (double)up(p.K, 16) > (double)most_blocks(256) * 256) return false;   // one launch
     const double few = few_time(p, few_best(p)), tiles = Times(p).least();
     return lying_time(p, lying_best(p)) > (few < tiles ? few : tiles) + 4.0 + ((double)p.M + p.N) * p.K / 2e6;
 }
@@ -675,9 +676,29 @@ template <typename T> hipError_t launch(Params p, void *ws, size_t ws_bytes, hip
     return start(any_k<T>, (unsigned)((long long)p.tm * p.tn), 256, 0, s, p);
 }
 
-}  // namespace
+// A launch holds fewer than 2^32 work-items, and the smallest tiles have 512 for
+// 16 x 16 outputs: y goes in parts that stay below that with every kernel (the
+// choice of one changes no bit), of whole columns where there are up to 2^15 rows.
+template <typename T> hipError_t parts(const Params &p, void *ws, size_t ws_bytes, hipStream_t s)
+{
+    const long long most = most_blocks(512), m16 = up(p.M, 16), n16 = up(p.N, 16);
+    if (m16 * n16 <= most) return launch<T>(p, ws, ws_bytes, s);
+    const long long rows = (m16 < 2048 ? m16 : 2048) * 16, columns = most / (rows / 16) * 16;
+    for (long long n = 0; n < p.N; n += columns)
+        for (long long m = 0; m < p.M; m += rows) {
+            Params q = p;
+            q.M = (int)(p.M - m < rows ? p.M - m : rows);
+            q.N = (int)(p.N - n < columns ? p.N - n : columns);
+            q.a += m * p.la, q.sa += m, q.w += n * p.lw, q.sw += n;
+            if (p.bias) q.bias += n;
+            q.y = (T *)p.y + m * p.ly + n;
+            const hipError_t e = launch<T>(q, ws, ws_bytes, s);
+            if (e != hipSuccess) return e;
+        }
+    return hipSuccess;
+}
 
-bool fits(const gconv_mm_q8_desc &d) { return (double)up(d.M, 16) * (double)up(d.N, 64) <= (double)kMaxGrid; }
+}  // namespace
 
 // For both operands' rows, whatever their addresses turn out to be.
 size_t workspace(const gconv_mm_q8_desc &d)
@@ -692,9 +713,9 @@ hipError_t run(const gconv_mm_q8_desc &d, const int8_t *a, const float *a_scale,
 {
     Params p{a, w, a_scale, w_scale, bias, y, d.a_stride, d.w_stride, d.y_stride, (int)d.M, (int)d.N, (int)d.K, 0, 0};
     switch (d.dtype) {
-    case GCONV_F32: return launch<float>(p, ws, ws_bytes, s);
-    case GCONV_F16: return launch<_Float16>(p, ws, ws_bytes, s);
-    default: return launch<__bf16>(p, ws, ws_bytes, s);
+    case GCONV_F32: return parts<float>(p, ws, ws_bytes, s);
+    case GCONV_F16: return parts<_Float16>(p, ws, ws_bytes, s);
+    default: return parts<__bf16>(p, ws, ws_bytes, s);
     }
 }
 

@@ -84,7 +84,7 @@ int check(const gconv_mm_q8_desc *d)
     if (d->a_stride < 0 || d->a_stride > kMostStride || d->w_stride < 0 || d->w_stride > kMostStride)
         return GCONV_ERR_BAD_DESC;
     if (d->y_stride < 0 || d->y_stride > kMostStride || (d->M > 1 && d->y_stride < d->N)) return GCONV_ERR_BAD_DESC;
-    return mmq8::fits(*d) ? GCONV_OK : GCONV_ERR_TOO_LARGE;
+    return GCONV_OK;
 }
 
 int status(hipError_t e) { return e == hipSuccess ? GCONV_OK : GCONV_ERR_LAUNCH; }

@@ -22,8 +22,7 @@ hipError_t start(void (*k)(KP...), unsigned grid, unsigned block, unsigned lds, 
     return hipLaunchKernel((const void *)k, dim3(grid), dim3(block), argv, lds, s);
 }
 
-constexpr long long kMaxGrid = 0x7fffffffll;   // workgroups in one launch
-// and work-items: a runtime refuses a grid whose blocks hold 2^32 or more
+// Workgroups of `block` threads in one launch: a runtime refuses 2^32 work-items or more.
 constexpr long long most_blocks(unsigned block) { return 0xffffffffll / block; }
 
 inline bool on(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
@@ -64,7 +63,6 @@ hipError_t run(const gconv_q8_desc &d, const void *x, const void *residual, cons
 
 namespace mmq8 {
 size_t workspace(const gconv_mm_q8_desc &d);
-bool fits(const gconv_mm_q8_desc &d);
 hipError_t run(const gconv_mm_q8_desc &d, const int8_t *a, const float *a_scale, const int8_t *w,
                const float *w_scale, const float *bias, void *y, void *ws, size_t ws_bytes, hipStream_t s);
 }

@@ -670,6 +670,23 @@ def test_product_offsets_past_32_bits():
     assert torch.equal(seq.matmul_q8(a, sa, w, sw, bias=bias, out=out), want)
 
 
+@pytest.mark.parametrize("M,N,K", [(1, (1 << 27) + 5, 16), (20, (1 << 26) + 37, 32), (3, (1 << 27) + 5, 17), ((1 << 26) + 37, 20, 16)])
+def test_product_larger_than_a_launch_holds(M, N, K):
+    """2^32 work-items and more in the kernel that a small product of these rows takes: rows, or columns, repeat ten."""
+    a, sa, w, sw, bias = operands(min(M, 20), min(N, 20), K)
+
+    def many(t, n):
+        return t if t.shape[0] >= n else t[:10].repeat((n // 10 + 1,) + (1,) * (t.dim() - 1))[:n]
+
+    want = check_product(a, sa, w, sw, bias, "bf16")
+    y = seq.matmul_q8(many(a, M), many(sa, M), many(w, N), many(sw, N), bias=many(bias, N))
+    for j in range(10):
+        if M > N:
+            assert (y[j::10] == want[j]).all()
+        else:
+            assert (y[:, j::10] == want[:, j:j + 1]).all()
+
+
 def test_product_does_not_depend_on_the_workspace():
     for M, N, K in ((1, 256, 8192), (16, 128, 4096), (40, 256, 4096), (130, 128, 8192)):
         a, sa, w, sw, bias = operands(M, N, K)
