@@ -527,6 +527,7 @@ template <typename T, int AL, int NW, int P> hipError_t few(Params p, hipStream_
 }
 template <typename T, int MT> hipError_t few_any(Params p, hipStream_t s)
 {
+    if (p.K < 16) return hipErrorInvalidValue;   // it reads 16 bytes of a row at once
     p.tm = (int)up(p.M, MT * 16);
     p.tn = (int)up(p.N, 16);
     return start(few_any_k<T, MT, 8>, (unsigned)((long long)p.tm * p.tn), 512, 0, s, p);
@@ -602,23 +603,20 @@ int few_best(const Params &p)   // the mt of the least time
     return best;
 }
 
+// What a call runs.  few: up to 8 rows, then 16 * mt a block; tiles: square; lying: rows read as they lie.
+enum Kernel { kFew8, kFew16, kFew32, kFew48, kFew64, kTile64, kTile128, kTile256, kLying16, kLying32, kLying64, kAny };
+
 // Rows in whole pieces.  Up to 8 rows a stage of the ring is smaller and there
 // are three: 1 x 8192 x 4096 8.5 -> 7.6 us.
-template <typename T> hipError_t pieces(const Params &p, hipStream_t s)
+Kernel of_pieces(const Params &p)
 {
     const Times t(p);
     const int mt = few_best(p);
-    if (few_time(p, mt) < t.least()) {
-        if (p.M <= 8) return few<T, 1, 8, 3>(p, s);
-        return mt == 1 ? few<T, 2, 8, 2>(p, s) : mt == 2 ? few<T, 4, 4, 2>(p, s)
-             : mt == 3 ? few<T, 6, 8, 2>(p, s) : few<T, 8, 4, 2>(p, s);
-    }
-    if (t.t64 <= t.t128 && t.t64 <= t.t256) return tiles<T, 64, 64, 32, 32, 10>(p, s);
-    if (t.t128 <= t.t256) return tiles<T, 128, 128, 64, 32, 5>(p, s);
-    return tiles<T, 256, 256, 128, 64, 5>(p, s);
+    if (few_time(p, mt) < t.least()) return p.M <= 8 ? kFew8 : (Kernel)(kFew16 + mt - 1);
+    return t.t64 <= t.t128 && t.t64 <= t.t256 ? kTile64 : t.t128 <= t.t256 ? kTile128 : kTile256;
 }
 
-// Rows that pieces() takes as they are: whole pieces of 16 bytes, and within a descriptor's reach.
+// Rows that few_k and tile_k take as they are: whole pieces of 16 bytes, and within a descriptor's reach.
 bool fine(const void *a, long long stride, int K) { return K % 16 == 0 && stride % 16 == 0 && on(a, 16) && stride < (1 << 22); }
 
 long long padded(int K) { return up(K, 16) * 16; }
@@ -641,7 +639,7 @@ double lying_time(const Params &p, int mt)
 int lying_best(const Params &p)
 {
     int best = 0;
-    if (p.K < 16) return best;   // few_any_k reads 16 bytes of a row at once
+    if (p.K < 16) return best;   // few_any refuses them
     for (int mt : kLying)
         if (lying_time(p, mt) < lying_time(p, best)) best = mt;
     return best;
@@ -653,44 +651,94 @@ bool pack_pays(const Params &p)
     return lying_time(p, lying_best(p)) > (few < tiles ? few : tiles) + 4.0 + ((double)p.M + p.N) * p.K / 2e6;
 }
 
+struct Route {
+    bool a_fine, w_fine, pack;   // pack: the operands that are not fine are copied first
+    Kernel kernel;
+};
+Route route(const Params &p, const void *ws, size_t ws_bytes)
+{
+    Route r{fine(p.a, p.la, p.K), fine(p.w, p.lw, p.K), false, kAny};
+    if (r.a_fine && r.w_fine) {
+        r.kernel = of_pieces(p);
+        return r;
+    }
+    const size_t need = ((r.a_fine ? 0 : (size_t)p.M) + (r.w_fine ? 0 : (size_t)p.N)) * padded(p.K);
+    r.pack = on(ws, 16) && ws_bytes >= need && pack_pays(p);
+    if (r.pack) {
+        Params q = p;
+        q.K = (int)padded(p.K);
+        r.kernel = of_pieces(q);
+    } else {
+        const int mt = lying_best(p);
+        r.kernel = mt == 0 ? kAny : mt == 1 ? kLying16 : mt == 2 ? kLying32 : kLying64;
+    }
+    return r;
+}
+
 template <typename T> hipError_t launch(Params p, void *ws, size_t ws_bytes, hipStream_t s)
 {
-    const bool a_fine = fine(p.a, p.la, p.K), w_fine = fine(p.w, p.lw, p.K);
-    if (a_fine && w_fine) return pieces<T>(p, s);
-    const long long kp = padded(p.K);
-    const size_t na = a_fine ? 0 : (size_t)p.M * kp, nw = w_fine ? 0 : (size_t)p.N * kp;
-    if (on(ws, 16) && ws_bytes >= na + nw && pack_pays(p)) {
+    const Route r = route(p, ws, ws_bytes);
+    if (r.pack) {
+        const long long kp = padded(p.K);
         const int per = (int)(kp / 16);
-        Pack q{{p.a, p.w}, {p.la, p.lw}, a_fine ? 0 : p.M * (long long)per, 0, (int8_t *)ws, p.K, per};
-        q.pieces = q.split + (w_fine ? 0 : p.N * (long long)per);
-        if (!a_fine) p.a = q.to, p.la = kp;
-        if (!w_fine) p.w = q.to + q.split * 16, p.lw = kp;
+        Pack q{{p.a, p.w}, {p.la, p.lw}, r.a_fine ? 0 : p.M * (long long)per, 0, (int8_t *)ws, p.K, per};
+        q.pieces = q.split + (r.w_fine ? 0 : p.N * (long long)per);
+        if (!r.a_fine) p.a = q.to, p.la = kp;
+        if (!r.w_fine) p.w = q.to + q.split * 16, p.lw = kp;
         const hipError_t e = start(pack_k, (unsigned)up(q.pieces, 256), 256, 0, s, q);
+        if (e != hipSuccess) return e;
         p.K = (int)kp;
-        return e != hipSuccess ? e : pieces<T>(p, s);
     }
-    const int mt = lying_best(p);
-    if (mt) return mt == 1 ? few_any<T, 1>(p, s) : mt == 2 ? few_any<T, 2>(p, s) : few_any<T, 4>(p, s);
+    switch (r.kernel) {
+    case kFew8: return few<T, 1, 8, 3>(p, s);
+    case kFew16: return few<T, 2, 8, 2>(p, s);
+    case kFew32: return few<T, 4, 4, 2>(p, s);
+    case kFew48: return few<T, 6, 8, 2>(p, s);
+    case kFew64: return few<T, 8, 4, 2>(p, s);
+    case kTile64: return tiles<T, 64, 64, 32, 32, 10>(p, s);
+    case kTile128: return tiles<T, 128, 128, 64, 32, 5>(p, s);
+    case kTile256: return tiles<T, 256, 256, 128, 64, 5>(p, s);
+    case kLying16: return few_any<T, 1>(p, s);
+    case kLying32: return few_any<T, 2>(p, s);
+    case kLying64: return few_any<T, 4>(p, s);
+    case kAny: break;
+    }
     p.tm = (int)up(p.M, 64);
     p.tn = (int)up(p.N, 64);
     return start(any_k<T>, (unsigned)((long long)p.tm * p.tn), 256, 0, s, p);
 }
+
+// The part of y that a launch may hold (parts() below).
+struct Part {
+    long long rows, columns;
+    explicit Part(const Params &p)
+    {
+        const long long most = most_blocks(512), m16 = up(p.M, 16), n16 = up(p.N, 16);
+        rows = p.M, columns = p.N;
+        if (m16 * n16 <= most) return;
+        rows = (m16 < 2048 ? m16 : 2048) * 16;
+        columns = most / (rows / 16) * 16;
+    }
+    Params at(const Params &p, long long m, long long n) const
+    {
+        Params q = p;
+        q.M = (int)(p.M - m < rows ? p.M - m : rows);
+        q.N = (int)(p.N - n < columns ? p.N - n : columns);
+        q.a += m * p.la, q.sa += m, q.w += n * p.lw, q.sw += n;
+        if (p.bias) q.bias += n;
+        return q;
+    }
+};
 
 // A launch holds fewer than 2^32 work-items, and the smallest tiles have 512 for
 // 16 x 16 outputs: y goes in parts that stay below that with every kernel (the
 // choice of one changes no bit), of whole columns where there are up to 2^15 rows.
 template <typename T> hipError_t parts(const Params &p, void *ws, size_t ws_bytes, hipStream_t s)
 {
-    const long long most = most_blocks(512), m16 = up(p.M, 16), n16 = up(p.N, 16);
-    if (m16 * n16 <= most) return launch<T>(p, ws, ws_bytes, s);
-    const long long rows = (m16 < 2048 ? m16 : 2048) * 16, columns = most / (rows / 16) * 16;
-    for (long long n = 0; n < p.N; n += columns)
-        for (long long m = 0; m < p.M; m += rows) {
-            Params q = p;
-            q.M = (int)(p.M - m < rows ? p.M - m : rows);
-            q.N = (int)(p.N - n < columns ? p.N - n : columns);
-            q.a += m * p.la, q.sa += m, q.w += n * p.lw, q.sw += n;
-            if (p.bias) q.bias += n;
+    const Part part(p);
+    for (long long n = 0; n < p.N; n += part.columns)
+        for (long long m = 0; m < p.M; m += part.rows) {
+            Params q = part.at(p, m, n);
             q.y = (T *)p.y + m * p.ly + n;
             const hipError_t e = launch<T>(q, ws, ws_bytes, s);
             if (e != hipSuccess) return e;
@@ -717,6 +765,20 @@ hipError_t run(const gconv_mm_q8_desc &d, const int8_t *a, const float *a_scale,
     case GCONV_F16: return parts<_Float16>(p, ws, ws_bytes, s);
     default: return parts<__bf16>(p, ws, ws_bytes, s);
     }
+}
+
+const char *kernel(const gconv_mm_q8_desc &d, const void *a, const void *w, const void *ws, size_t ws_bytes)
+{
+    static const char *const names[2][kAny + 1] = {
+        {"few_k 8", "few_k 16", "few_k 32", "few_k 48", "few_k 64", "tile_k 64", "tile_k 128", "tile_k 256", "few_any_k 16",
+         "few_any_k 32", "few_any_k 64", "any_k"},
+        {"pack_k, few_k 8", "pack_k, few_k 16", "pack_k, few_k 32", "pack_k, few_k 48", "pack_k, few_k 64",
+         "pack_k, tile_k 64", "pack_k, tile_k 128", "pack_k, tile_k 256"}};
+    if (d.M == 0) return "";
+    const Params p{(const int8_t *)a, (const int8_t *)w, nullptr, nullptr, nullptr, nullptr, d.a_stride, d.w_stride,
+                   d.y_stride, (int)d.M, (int)d.N, (int)d.K, 0, 0};
+    const Route r = route(Part(p).at(p, 0, 0), ws, ws_bytes);
+    return names[r.pack][r.kernel];
 }
 
 }  // namespace mmq8

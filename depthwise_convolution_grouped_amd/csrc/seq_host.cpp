@@ -171,6 +171,12 @@ GCONV_API int gconv_matmul_q8_workspace(const gconv_mm_q8_desc *d, size_t *bytes
     return GCONV_OK;
 }
 
+GCONV_API const char *gconv_matmul_q8_kernel(const gconv_mm_q8_desc *d, const void *a, const void *w,
+                                             const void *workspace, size_t workspace_bytes)
+{
+    return check(d) == GCONV_OK ? mmq8::kernel(*d, a, w, workspace, workspace ? workspace_bytes : 0) : "";
+}
+
 GCONV_API int gconv_matmul_q8(const gconv_mm_q8_desc *d, const int8_t *a, const float *a_scale, const int8_t *w,
                               const float *w_scale, const float *bias, void *y, void *workspace,
                               size_t workspace_bytes, void *stream)

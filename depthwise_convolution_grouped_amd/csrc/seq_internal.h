@@ -63,6 +63,7 @@ hipError_t run(const gconv_q8_desc &d, const void *x, const void *residual, cons
 
 namespace mmq8 {
 size_t workspace(const gconv_mm_q8_desc &d);
+const char *kernel(const gconv_mm_q8_desc &d, const void *a, const void *w, const void *ws, size_t ws_bytes);
 hipError_t run(const gconv_mm_q8_desc &d, const int8_t *a, const float *a_scale, const int8_t *w,
                const float *w_scale, const float *bias, void *y, void *ws, size_t ws_bytes, hipStream_t s);
 }

@@ -54,8 +54,8 @@ EXPORTS = ("gconv_validate", "gconv_out_dims", "gconv_select_path", "gconv_path_
            "gconv_bwd_data_workspace", "gconv_bwd_data", "gconv_bwd_data_direct",
            "gconv_bwd_weight_workspace", "gconv_bwd_weight", "gconv_bwd_weight_noalloc",
            "gconv_glr_fwd_workspace", "gconv_glr_fwd", "gconv_glr_bwd_workspace", "gconv_glr_bwd",
-           "gconv_rmsnorm_q8", "gconv_quant_q8", "gconv_matmul_q8_workspace", "gconv_matmul_q8",
-           "gconv_status_str", "gconv_path_name", "gconv_abi_version")
+           "gconv_rmsnorm_q8", "gconv_quant_q8", "gconv_matmul_q8_workspace", "gconv_matmul_q8_kernel",
+           "gconv_matmul_q8", "gconv_status_str", "gconv_path_name", "gconv_abi_version")
 
 
 class GconvUnavailable(RuntimeError):
@@ -150,6 +150,8 @@ def lib():
     L.gconv_quant_q8.argtypes = [pq] + [vp] * 4
     L.gconv_matmul_q8_workspace.argtypes = [pm, psz]
     L.gconv_matmul_q8.argtypes = [pm] + [vp] * 6 + [vp, sz, vp]
+    L.gconv_matmul_q8_kernel.argtypes = [pm, vp, vp, vp, sz]
+    L.gconv_matmul_q8_kernel.restype = ctypes.c_char_p
     for name in ("gconv_glr_fwd_workspace", "gconv_glr_fwd", "gconv_glr_bwd_workspace", "gconv_glr_bwd",
                  "gconv_rmsnorm_q8", "gconv_quant_q8", "gconv_matmul_q8_workspace", "gconv_matmul_q8"):
         getattr(L, name).restype = ctypes.c_int

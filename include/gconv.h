@@ -449,6 +449,13 @@ typedef struct gconv_mm_q8_desc {
  * 16, or an address that is none).  A call whose rows are uses none. */
 int gconv_matmul_q8_workspace(const gconv_mm_q8_desc *d, size_t *bytes);
 
+/* Names the kernels that such a call runs, and the rows of a block (few_k,
+ * few_any_k) or the side of a tile: "few_k 16", "pack_k, tile_k 128".  A static
+ * string, never NULL; empty where the call runs none.  Of the addresses only the
+ * alignment counts.  (A product larger than a launch goes in parts: its first.) */
+const char *gconv_matmul_q8_kernel(const gconv_mm_q8_desc *d, const void *a, const void *w,
+                                   const void *workspace, size_t workspace_bytes);
+
 /* workspace may be NULL or smaller than the query's: such rows are then read
  * as they lie.  The result's bits do not depend on it, nor on the strides. */
 int gconv_matmul_q8(const gconv_mm_q8_desc *d, const int8_t *a, const float *a_scale,

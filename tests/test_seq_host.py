@@ -206,6 +206,32 @@ def test_product_refuses_bad_pointers():
     assert product(mm_desc(M=0), a=None, sa=None, w=None, sw=None, y=None) == G.GCONV_OK
 
 
+def kernel(d, a=P, w=P, workspace=True):
+    n = ctypes.c_size_t()
+    assert G.lib().gconv_matmul_q8_workspace(ctypes.byref(d), ctypes.byref(n)) == G.GCONV_OK
+    return G.lib().gconv_matmul_q8_kernel(ctypes.byref(d), a, w, P if workspace else None, n.value).decode()
+
+
+@pytest.mark.parametrize("K", list(range(1, 16)))
+def test_rows_shorter_than_a_load_stay_with_the_kernel_that_takes_them(K):
+    """few_any_k reads the 16 bytes that end with a row's; a shorter row has none before it."""
+    for M in (1, 15, 16, 33, 64, 300, 2048, 100000):
+        for N in (1, 17, 1000, 4096):
+            for stride in (K, K + 1, 64):
+                for at in (P, P + 1):
+                    for ws in (False, True):
+                        name = kernel(mm_desc(M=M, N=N, K=K, a=stride, w=stride), a=at, w=at, workspace=ws)
+                        assert name == "any_k" or name.startswith("pack_k, ") and ws, (M, N, stride, name)
+
+
+def test_kernel_names():
+    assert kernel(mm_desc(M=1, N=64, K=32)) == "few_k 8"
+    assert kernel(mm_desc(M=1, N=64, K=32), a=P + 1) == "few_any_k 16"
+    for d in (mm_desc(M=0), mm_desc(K=0), mm_desc(M=1 << 31)):
+        assert G.lib().gconv_matmul_q8_kernel(ctypes.byref(d), P, P, None, 0) == b""
+    assert G.lib().gconv_matmul_q8_kernel(None, P, P, None, 0) == b""
+
+
 def test_status_of_the_workspace():
     assert G.gconv_status_str(G.GCONV_ERR_WORKSPACE) != G.gconv_status_str(-99)
 
