@@ -409,7 +409,7 @@ template <typename T, bool SPLIT, bool FAR> __global__ __launch_bounds__(kLanes 
 #pragma unroll
         for (int s = 0; s < S; ++s) {
             hs = fmaf(a[s], hs, u[s]);
-            if (FULL || ts + s < ce) y.store(w0 + s, from_f32<T>(FULL || ts + s < n ? hs : 0.0f));
+            if (FULL || ts + s < ce) y.store(w0 + s, rounded<T>(FULL || ts + s < n ? hs : 0.0f));
         }
         buf ^= 1;
     };
@@ -420,7 +420,7 @@ template <typename T, bool SPLIT, bool FAR> __global__ __launch_bounds__(kLanes 
         const int w0 = wave * S, ts = t0 + w0;
         const In y(p.y, p.sy, b, t0, ch, live);
         for (int s = 0; s < S; ++s)
-            if (ts + s < ce) y.store(w0 + s, from_f32<T>(0.0f));
+            if (ts + s < ce) y.store(w0 + s, rounded<T>(0.0f));
         keep(ts, 0.0f);
     }
     // the block that holds the row's end has its last state
@@ -466,7 +466,7 @@ template <typename T> __global__ __launch_bounds__(64) void fwd_serial_k(Few p)
             const float si = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * to_f32(i[t * p.si[1]])));
             h = fmaf(g.a, h, __builtin_amdgcn_sqrtf(g.w) * si * to_f32(x[t * p.sx[1]]));
         }
-        y[t * p.sy[1]] = from_f32<T>(t < n ? h : 0.0f);
+        y[t * p.sy[1]] = rounded<T>(t < n ? h : 0.0f);
     }
     if (p.h_last) p.h_last[row] = h;
 }
@@ -597,9 +597,9 @@ template <typename T, bool FAR, bool AHEAD> __global__ __launch_bounds__(kLanes 
         const In dx(p.dx, p.sdx, b, t0, ch, live), dr(p.dr, p.sdr, b, t0, ch, live), di(p.di, p.sdi, b, t0, ch, live);
         for (int k = wave * S; k < wave * S + S; ++k)
             if (t0 + k < ce) {
-                dx.store(k, from_f32<T>(0.0f));
-                dr.store(k, from_f32<T>(0.0f));
-                di.store(k, from_f32<T>(0.0f));
+                dx.store(k, rounded<T>(0.0f));
+                dr.store(k, rounded<T>(0.0f));
+                di.store(k, rounded<T>(0.0f));
             }
     }
     if (AHEAD && t0 >= cs) load(t0, std::false_type());
@@ -663,9 +663,9 @@ template <typename T, bool FAR, bool AHEAD> __global__ __launch_bounds__(kLanes 
             const float w = in ? Rs * la[s] * d[s] : 0.0f, gin = in ? g : 0.0f;
             sum += w;
             if (FULL || ts + s < ce) {
-                dx.store(w0 + s, from_f32<T>(gin * ms[s]));
-                dr.store(w0 + s, from_f32<T>(nr[s] * (w * kLn2)));
-                di.store(w0 + s, from_f32<T>(gin * ni[s]));
+                dx.store(w0 + s, rounded<T>(gin * ms[s]));
+                dr.store(w0 + s, rounded<T>(nr[s] * (w * kLn2)));
+                di.store(w0 + s, rounded<T>(gin * ni[s]));
             }
         }
         buf ^= 1;

@@ -42,7 +42,7 @@ template <typename T> __device__ __forceinline__ void store4(const Params &p, in
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         if (n + j >= p.N) return;
-        y[j] = from_f32<T>(scaled(acc[j], sa, p.sw[n + j], p.bias ? p.bias[n + j] : 0.0f));
+        y[j] = rounded<T>(scaled(acc[j], sa, p.sw[n + j], p.bias ? p.bias[n + j] : 0.0f));
     }
 }
 
@@ -319,10 +319,10 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64) void tile_k(Params p)
                 const int c = i * 32 + g * 8 + half * 4;
                 const float4 w = *(const float4 *)(sw + c), b = *(const float4 *)(bias + c);
                 struct alignas(4 * sizeof(T)) { T v[4]; } o;
-                o.v[0] = from_f32<T>(scaled(acc[i][j][g * 4], sa[j], w.x, b.x));
-                o.v[1] = from_f32<T>(scaled(acc[i][j][g * 4 + 1], sa[j], w.y, b.y));
-                o.v[2] = from_f32<T>(scaled(acc[i][j][g * 4 + 2], sa[j], w.z, b.z));
-                o.v[3] = from_f32<T>(scaled(acc[i][j][g * 4 + 3], sa[j], w.w, b.w));
+                o.v[0] = rounded<T>(scaled(acc[i][j][g * 4], sa[j], w.x, b.x));
+                o.v[1] = rounded<T>(scaled(acc[i][j][g * 4 + 1], sa[j], w.y, b.y));
+                o.v[2] = rounded<T>(scaled(acc[i][j][g * 4 + 2], sa[j], w.z, b.z));
+                o.v[3] = rounded<T>(scaled(acc[i][j][g * 4 + 3], sa[j], w.w, b.w));
                 __builtin_memcpy(__builtin_assume_aligned(mine + lane % 32 * PITCH + c * sizeof(T), 4 * sizeof(T)), &o, sizeof(o));
             }
         }
@@ -411,7 +411,7 @@ template <typename T, int AL, int NW, int P> __global__ __launch_bounds__(NW * 6
         int sum = 0;
 #pragma unroll
         for (int v = 0; v < NW; ++v) sum += part[v * MT * 256 + o];
-        ((T *)p.y)[m * p.ly + n] = from_f32<T>(scaled(sum, sa[j], sw[j], bias[j]));
+        ((T *)p.y)[m * p.ly + n] = rounded<T>(scaled(sum, sa[j], sw[j], bias[j]));
     }
 }
 
@@ -515,7 +515,7 @@ template <typename T, int MT, int NW> __global__ __launch_bounds__(NW * 64) void
         int sum = 0;
 #pragma unroll
         for (int w = 0; w < NW; ++w) sum += part[w * MT * 256 + o];
-        ((T *)p.y)[m * p.ly + n] = from_f32<T>(scaled(sum, sa[j], sw[j], bias[j]));
+        ((T *)p.y)[m * p.ly + n] = rounded<T>(scaled(sum, sa[j], sw[j], bias[j]));
     }
 }
 

@@ -5,6 +5,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include <hip/hip_runtime.h>
 
 #include "gconv.h"
@@ -27,6 +29,16 @@ constexpr long long most_blocks(unsigned block) { return 0xffffffffll / block; }
 
 inline bool on(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 inline long long up(long long a, long long b) { return (a + b - 1) / b; }
+
+// v, an fp32 number, in T.  A multiply-add right before a conversion to fp16 may
+// become one instruction, which rounds the exact sum to fp16 without a stop at
+// fp32; whether it does goes by what else is in the block, so the bits of a
+// result would depend on the kernel.  Behind the barrier it is always two.
+template <typename T> __device__ __forceinline__ T rounded(float v)
+{
+    if constexpr (std::is_same<T, _Float16>::value) asm("" : "+v"(v));
+    return (T)v;
+}
 
 namespace glr {
 struct Fwd {

@@ -377,6 +377,21 @@ def test_recurrence_more_chunks_than_a_launch_holds():
     assert abs(float(ends[0]) - want) <= tol + half and abs(float(ends[1]) - want) <= tol + half
 
 
+@pytest.mark.parametrize("t", ["f16", "bf16"])
+@pytest.mark.parametrize("B,L,D,lengths", [(2, 2000, 200, None), (3, 1000, 70, [1000, 130, 777]), (9, 100, 4000, None), (3, 7, 500, None)])
+def test_recurrence_rounds_what_fp32_holds(B, L, D, lengths, t):
+    """16-bit outputs are the fp32 call's, rounded, whole and split, in every block."""
+    k = Case(B, L, D, t, lengths)
+    y, last, states = seq.glr_fwd(*k.args, h0=k.h0, lengths=k.n, save=True)
+    wide = [v.float() for v in k.args]
+    y32, last32, states32 = seq.glr_fwd(*wide, h0=k.h0, lengths=k.n, save=True)
+    assert torch.equal(y, y32.to(TYPES[t])) and torch.equal(last, last32) and torch.equal(states, states32)
+    got = seq.glr_bwd(k.dy, *k.args, states, lengths=k.n, dh_last=k.dh)
+    want = seq.glr_bwd(k.dy.float(), *wide, states, lengths=k.n, dh_last=k.dh)
+    for a, b in zip(got, want):
+        assert torch.equal(a, b.to(a.dtype))
+
+
 def test_recurrence_gradient_against_differences():
     """The fp32 forward's own central differences along random directions.
 
@@ -641,6 +656,20 @@ def test_product_few_rows_as_they_lie(M, K):
         none = torch.empty(0, dtype=torch.uint8, device="cuda")
         check_product(wa, sa, ww, sw, bias, "f32", workspace=none)
         check_product(wa, sa, ww, sw, bias, "f32")
+
+
+@pytest.mark.parametrize("M,N,K", [(5, 408, 240), (14, 500, 1040), (51, 2172, 368), (1024, 1024, 512), (2048, 2048, 256),
+                                   (3000, 3001, 144), (2831, 334, 68), (210, 1646, 461), (846, 900, 589)])
+@pytest.mark.parametrize("t", ["f16", "bf16"])
+def test_product_rounds_what_fp32_holds(M, N, K, t):
+    """16-bit outputs are the fp32 call's, rounded, whichever kernel, workspace or stride of y a call has."""
+    a, sa, w, sw, bias = operands(M, N, K)
+    want = seq.matmul_q8(a, sa, w, sw, bias=bias, out_dtype=torch.float32).to(TYPES[t])
+    none = torch.empty(0, dtype=torch.uint8, device="cuda")
+    for ws in (None, none):
+        assert torch.equal(seq.matmul_q8(a, sa, w, sw, bias=bias, out_dtype=TYPES[t], workspace=ws), want)
+    out = torch.empty(M, N + 1, dtype=TYPES[t], device="cuda")[:, :N]
+    assert torch.equal(seq.matmul_q8(a, sa, w, sw, bias=bias, out=out), want)
 
 
 @pytest.mark.parametrize("M", [1, 40, 260])
