@@ -672,6 +672,67 @@ def test_product_rounds_what_fp32_holds(M, N, K, t):
     assert torch.equal(seq.matmul_q8(a, sa, w, sw, bias=bias, out=out), want)
 
 
+def route(a, w, workspace=True):
+    """(the kernels that a product of a and w runs, the bytes of workspace that it can use)."""
+    (M, K), N = a.shape, w.shape[0]
+    d = G.gconv_mm_q8_desc(dtype=G.GCONV_BF16, M=M, N=N, K=K, a_stride=a.stride(0), w_stride=w.stride(0), y_stride=N)
+    n = ctypes.c_size_t()
+    assert G.lib().gconv_matmul_q8_workspace(ctypes.byref(d), ctypes.byref(n)) == G.GCONV_OK
+    name = G.lib().gconv_matmul_q8_kernel(ctypes.byref(d), a.data_ptr(), w.data_ptr(), 16 if workspace else None, n.value)
+    return name.decode(), n.value
+
+
+ROUTES = [("few_k 8", 5, 408, 240), ("few_k 16", 14, 500, 1040), ("few_k 32", 37, 1503, 640), ("few_k 48", 160, 974, 336),
+          ("few_k 64", 51, 2172, 368), ("tile_k 64", 819, 1099, 176), ("tile_k 64", 1024, 1024, 4096),
+          ("tile_k 128", 2048, 2048, 256), ("tile_k 128", 2300, 2201, 272), ("tile_k 128", 3479, 694, 528),
+          ("tile_k 128", 6573, 257, 16), ("tile_k 256", 4096, 4096, 256), ("tile_k 256", 3000, 3001, 144),
+          ("tile_k 256", 4613, 1727, 16), ("tile_k 256", 7236, 1295, 576), ("any_k", 2831, 334, 68), ("any_k", 38, 2860, 17),
+          ("few_any_k 16", 40, 3000, 2001), ("few_any_k 32", 210, 1646, 461), ("few_any_k 64", 120, 4000, 2001),
+          ("few_any_k 64", 49, 6246, 257), ("pack_k, few_k 16", 1165, 210, 7635), ("pack_k, few_k 32", 390, 659, 3851),
+          ("pack_k, few_k 48", 322, 395, 3981), ("pack_k, few_k 64", 531, 340, 6380), ("pack_k, tile_k 64", 846, 900, 589),
+          ("pack_k, tile_k 64", 200, 4000, 4095), ("pack_k, tile_k 128", 2824, 5559, 18),
+          ("pack_k, tile_k 128", 2048, 2048, 2047), ("pack_k, tile_k 256", 4176, 2359, 17),
+          ("pack_k, tile_k 256", 4100, 4100, 200)]
+
+
+@pytest.mark.parametrize("name,M,N,K", ROUTES)
+def test_product_every_kernel(name, M, N, K):
+    """Random codes through each kernel, in every type, with rows of y on and off the 16-byte grid; where rows are copied
+    first, the same bits without a workspace."""
+    a, sa, w, sw, bias = operands(M, N, K)
+    assert route(a, w)[0] == name
+    want, tol = ref.matmul_q8(a.cpu().numpy(), f64(sa), w.cpu().numpy(), f64(sw), f64(bias))
+    for t in TYPES.values():
+        y = seq.matmul_q8(a, sa, w, sw, bias=bias, out_dtype=t)
+        near(y, want, tol, "%s %s" % (name, t))
+        wide = torch.full((M, N + 3), 3.0, dtype=t, device="cuda")
+        seq.matmul_q8(a, sa, w, sw, bias=bias, out=wide[:, 1:N + 1])
+        assert torch.equal(wide[:, 1:N + 1], y) and (wide[:, :1] == 3).all() and (wide[:, N + 1:] == 3).all()
+        if name.startswith("pack_k"):
+            none = torch.empty(0, dtype=torch.uint8, device="cuda")
+            assert not route(a, w, False)[0].startswith("pack_k") and route(a, w)[1] > 0
+            assert torch.equal(y, seq.matmul_q8(a, sa, w, sw, bias=bias, out_dtype=t, workspace=none))
+
+
+@pytest.mark.parametrize("which", ["a", "w"])
+@pytest.mark.parametrize("M,N,K", [(2048, 2048, 512), (700, 1500, 1024)])
+def test_product_copies_one_operand(M, N, K, which):
+    """Only the operand whose rows are not whole pieces is copied; its rows lie apart, from an odd address."""
+    a, sa, w, sw, bias = operands(M, N, K)
+    want = check_product(a, sa, w, sw, bias, "f32")
+    n = M if which == "a" else N
+    wide = torch.full((n, K + 19), 55, dtype=torch.int8, device="cuda")
+    wide[:, 3:K + 3] = a if which == "a" else w
+    if which == "a":
+        a = wide[:, 3:K + 3]
+    else:
+        w = wide[:, 3:K + 3]
+    assert route(a, w)[0].startswith("pack_k, ")
+    room = torch.empty(n * K, dtype=torch.uint8, device="cuda")   # enough for this operand alone
+    assert torch.equal(seq.matmul_q8(a, sa, w, sw, bias=bias, out_dtype=torch.float32, workspace=room), want)
+    assert torch.equal(seq.matmul_q8(a, sa, w, sw, bias=bias, out_dtype=torch.float32), want)
+
+
 @pytest.mark.parametrize("M", [1, 40, 260])
 def test_product_largest_sums(M):
     """-128 times -128 along the longest K stays below 2^31; the whole range of codes."""
