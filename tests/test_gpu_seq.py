@@ -135,6 +135,31 @@ def test_recurrence_long_few_channels(split):
     c.check(split=split, what="ragged split %s" % split)
 
 
+def shapes(B, L, D):
+    """(forward split, backward chunks of more than one 64-step stride or none) of the workspace queries."""
+    d = G.gconv_glr_desc(dtype=G.GCONV_F32, c=8.0, B=B, L=L, D=D)
+    for name in ("x", "r", "i", "y", "dx", "dr", "di"):
+        setattr(d, name + "_stride", (ctypes.c_int64 * 2)(L * D, D))
+    fwd, bwd, least = (ctypes.c_size_t() for _ in range(3))
+    assert G.lib().gconv_glr_fwd_workspace(ctypes.byref(d), ctypes.byref(fwd)) == G.GCONV_OK
+    assert G.lib().gconv_glr_bwd_workspace(ctypes.byref(d), ctypes.byref(bwd), ctypes.byref(least)) == G.GCONV_OK
+    chunks = bwd.value // (12 * B * D) if bwd.value > least.value else 1   # a pair and a sum for each
+    return fwd.value > 0, chunks
+
+
+@pytest.mark.parametrize("t", list(TYPES))
+@pytest.mark.parametrize("B,L,D,lengths,split,chunks", [
+    (8, 150, 2048, None, False, 1),                         # 256 blocks: a stride's loads ahead of it
+    (20, 200, 900, [200, 0, 1, 199, 64, 65] + [137] * 14, False, 1),    # 300 blocks, whole
+    (20, 400, 900, None, True, 1),                          # the same with the forward pass split
+    (9, 300, 4000, None, False, 1),                         # 567 blocks, both whole over several strides
+    (10, 700, 1280, [700, 1, 0, 256, 257, 511, 512, 513, 640, 699], True, 3),   # backward chunks of 256 steps
+    (1, 33000, 24, None, True, 258)])                       # and of 128
+def test_recurrence_every_form(B, L, D, lengths, split, chunks, t):
+    assert shapes(B, L, D) == (split, chunks)
+    Case(B, L, D, t, lengths=lengths).check(what="%d %d %d %s" % (B, L, D, t))
+
+
 def test_recurrence_extreme_gates():
     """Gates at and past fp32's exponential range, decays of 0 and 1, other values of c."""
     for c in (0.5, 30.0):
@@ -392,6 +417,24 @@ def test_recurrence_rounds_what_fp32_holds(B, L, D, lengths, t):
         assert torch.equal(a, b.to(a.dtype))
 
 
+@pytest.mark.parametrize("t,L,D,far", [("f32", 500, 24, 1 << 22), ("f16", 500, 24, 1 << 23), ("f32", 20, 70, 1 << 26),
+                                       ("f16", 5, 70, 1 << 30)])
+def test_recurrence_far_rows_in_every_form(t, L, D, far):
+    """Steps so far apart that a block's offsets pass 31 bits: split, whole and a few steps, forward and backward."""
+    big = torch.empty((L - 1) * far + 8 * D, dtype=TYPES[t], device="cuda")
+    rows = [big.as_strided((1, L, D), (0, far, 1), k * D) for k in range(8)]
+    k = Case(1, L, D, t)
+    for v, w in zip(rows, (k.x, k.r, k.i, k.dy)):
+        v.copy_(w)
+    x, r, i, dy, out, dx, dr, di = rows
+    want, last, states = seq.glr_fwd(*k.args, h0=k.h0, save=True)
+    got, last2, states2 = seq.glr_fwd(x, r, i, k.lam, h0=k.h0, out=out, save=True)
+    assert torch.equal(got, want) and torch.equal(last, last2) and torch.equal(states, states2)
+    want = seq.glr_bwd(k.dy, *k.args, states, dh_last=k.dh)
+    got = seq.glr_bwd(dy, x, r, i, k.lam, states, dh_last=k.dh, dx=dx, dr=dr, di=di)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_recurrence_gradient_against_differences():
     """The fp32 forward's own central differences along random directions.
 
@@ -509,6 +552,13 @@ def test_rows(M, D, t):
     check_rows(x, q, scale, total, w)
     q, scale = seq.quant_q8(x)
     check_rows(x, q, scale, None)
+
+
+@pytest.mark.parametrize("t", list(TYPES))
+@pytest.mark.parametrize("M,D", [(3, 2049), (3, 2056), (2, 3001), (5, 4096), (2, 4097), (2, 12000)])
+def test_rows_every_kernel(M, D, t):
+    """The lengths between test_rows's: two pieces a thread from 2049 to 4096, and the others' ends."""
+    test_rows(M, D, t)
 
 
 @pytest.mark.parametrize("D", [40, 47, 9000])
