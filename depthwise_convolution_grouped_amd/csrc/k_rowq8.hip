@@ -17,6 +17,12 @@ namespace rowq8 {
 namespace {
 
 constexpr float kLeast = 7.52316385e-37f;   // 2^-120: 127 / kLeast is still finite
+// A mean of squares (and eps) below kFaint may have lost bits to fp32's range:
+// 2^-126, a square's loss, is 2^-26 of it.  Such a row is summed again times kUp:
+// its sum, below 2^-69 for any D, stays finite times kUp^2, and the square of
+// fp32's least value, 2^-298, is 2^-110 then.
+constexpr float kFaint = 7.88860905e-31f;   // 2^-100
+constexpr float kUp = 1.98070406e28f;       // 2^94
 
 template <typename T, int V> struct alignas(sizeof(T) * V) Pack {
     T v[V];
@@ -57,13 +63,25 @@ template <int NT> __device__ __forceinline__ void reduce(float &sq, unsigned &to
     for (int w = 1; w < NW; ++w) sq += ls[w], top = umax(top, lt[w]);
 }
 
-// The row's scale and the factor from s * weight to q.
-template <bool NORM> __device__ __forceinline__ void factors(const Params &p, float sq, unsigned top, float &scale, float &k)
+// Whether the sum of squares has to be taken again, the same in every thread.
+__device__ __forceinline__ bool faint(const Params &p, float sq, unsigned top)
+{
+    return sq * p.inv_d + p.eps < kFaint && top < 0x7f800000u && __uint_as_float(top) >= kLeast;
+}
+
+// The row's scale and the factor from s * weight to q.  up: sq is that of s * kUp.
+template <bool NORM> __device__ __forceinline__ void factors(const Params &p, float sq, unsigned top, bool up, float &scale, float &k)
 {
     const float big = __uint_as_float(top);
-    const float norm = NORM ? 1.0f / sqrtf(sq * p.inv_d + p.eps) : 1.0f;
     const bool bad = top >= 0x7f800000u || (NORM && !(sq < __builtin_inff()));
-    scale = bad ? __builtin_nanf("") : big < kLeast ? 0.0f : big * norm * (1.0f / 127.0f);
+    if (NORM && up) {   // big, the factor and kUp may pass fp32's range by pairs
+        const float norm = 1.0f / sqrtf(sq * p.inv_d + p.eps * kUp * kUp);
+        scale = (float)((double)big * (double)norm * ((double)kUp / 127.0));
+    } else {
+        const float norm = NORM ? 1.0f / sqrtf(sq * p.inv_d + p.eps) : 1.0f;
+        scale = big * norm * (1.0f / 127.0f);
+    }
+    scale = bad ? __builtin_nanf("") : big < kLeast ? 0.0f : scale;
     k = bad || big < kLeast ? 0.0f : 127.0f / big;
 }
 // q of one value: a NaN or Inf of a row without a scale gives 0.
@@ -97,6 +115,13 @@ template <bool ALIGNED, typename T> __device__ __forceinline__ void store8(T *ro
         for (int j = 0; j < 8; ++j)
             if (ch + j < D) row[ch + j] = v.v[j];
     }
+}
+
+// s of one channel once more, after the thread has stored its sums (which may lie over x or the residual).
+template <typename T> __device__ __forceinline__ float stored_sum(const T *x, const T *res, const T *sum, long long ch)
+{
+    if (sum) return to_f32(sum[ch]);
+    return res ? to_f32(from_f32<T>(to_f32(x[ch]) + to_f32(res[ch]))) : to_f32(x[ch]);
 }
 
 // A row in registers: NT threads with NV pieces of eight channels each.
@@ -142,8 +167,24 @@ template <typename T, int NT, int NV, bool NORM, bool ALIGNED> __global__ __laun
         }
     }
     reduce<NT>(sq, top);
+    const bool up = NORM && faint(p, sq, top);
+    if (up) {
+        sq = 0.0f;
+#pragma unroll 1
+        for (int j = 0; j < NV; ++j) {
+            const int c0 = (j * NT + (int)threadIdx.x) * 8;
+#pragma unroll 1
+            for (int ch = c0; ch < c0 + 8 && ch < p.D; ++ch) {
+                const float t = stored_sum(x, res, sum, ch) * kUp;
+                sq = fmaf(t, t, sq);
+            }
+        }
+        __syncthreads();   // the first sums have been read
+        unsigned none = 0;
+        reduce<NT>(sq, none);
+    }
     float scale, k;
-    factors<NORM>(p, sq, top, scale, k);
+    factors<NORM>(p, sq, top, up, scale, k);
     if (threadIdx.x == 0) p.scale[m] = scale;
     int8_t *q = p.q + m * p.sq;
 #pragma unroll
@@ -180,18 +221,22 @@ template <typename T, bool NORM> __global__ __launch_bounds__(1024) void long_k(
         top = umax(top, mag(f));
     }
     reduce<1024>(sq, top);
+    const bool up = NORM && faint(p, sq, top);
+    if (up) {
+        sq = 0.0f;
+        for (long long ch = threadIdx.x; ch < p.D; ch += 1024) {
+            const float t = stored_sum(x, res, sum, ch) * kUp;
+            sq = fmaf(t, t, sq);
+        }
+        __syncthreads();   // the first sums have been read
+        unsigned none = 0;
+        reduce<1024>(sq, none);
+    }
     float scale, k;
-    factors<NORM>(p, sq, top, scale, k);
+    factors<NORM>(p, sq, top, up, scale, k);
     if (threadIdx.x == 0) p.scale[m] = scale;
     for (long long ch = threadIdx.x; ch < p.D; ch += 1024) {   // each thread reads what it wrote itself
-        T t;
-        if (NORM && sum) t = sum[ch];
-        else {
-            t = x[ch];
-            if (NORM && res) t = from_f32<T>(to_f32(t) + to_f32(res[ch]));
-        }
-        float f = to_f32(t);
-        if (NORM) f *= p.weight[ch];
+        float f = NORM ? stored_sum(x, res, sum, ch) * p.weight[ch] : to_f32(x[ch]);
         p.q[m * p.sq + ch] = (int8_t)code(f, k);
     }
 }

@@ -414,8 +414,9 @@ int gconv_glr_bwd(const gconv_glr_desc *d, const void *x, const void *r, const v
  *
  * A row whose largest |v|, before the division by the norm, is below 2^-120
  * has scale 0 and codes 0; a row with an Inf or NaN has scale NaN and codes
- * 0, so that a product with it is NaN.  The sums are fp32: a row of fp32
- * values whose sum of squares passes fp32's range has scale NaN as well.
+ * 0, so that a product with it is NaN.  The sums are fp32: a row of which the
+ * sum of squares or an s * weight passes fp32's range has scale NaN as well.
+ * (Squares below its range are kept: the row is summed again, scaled up.)
  * M >= 0 rows of D >= 1 channels, both at most 2^31 - 1024; strides between rows in elements; q and
  * sum rows may not overlap.  sum (NULL = not wanted; needs residual) may be
  * the same memory and stride as residual or x. */

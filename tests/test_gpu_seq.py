@@ -616,6 +616,27 @@ def test_rows_without_values(D):
     assert torch.equal(seq.quant_q8(big)[0], torch.full((1, D), 127, dtype=torch.int8, device="cuda"))
 
 
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+@pytest.mark.parametrize("D", [64, 65, 1000, 3000, 8000, 9001, 20000])
+@pytest.mark.parametrize("eps", [0.0, float(np.float32(1e-44)), float(np.float32(1e-38))])
+def test_rows_of_faint_values(D, t, eps):
+    """Values whose squares, and eps, are below fp32's range; the largest stays above 2^-120."""
+    g = torch.Generator(device="cuda").manual_seed(D)
+    size = torch.tensor([1e-14, 1e-16, 1e-18, 1e-20, 1e-22, 1e-25, 1e-30, 2e-36], device="cuda")
+    x, res = (size[:, None] * torch.randn(8, D, device="cuda", generator=g) for _ in range(2))
+    x, res = x.to(TYPES[t]), res.to(TYPES[t])
+    w = 1 + 0.3 * torch.randn(D, device="cuda", generator=g)
+    check_rows(x, *seq.rmsnorm_q8(x, w, eps=eps), w, eps=eps)
+    got = seq.rmsnorm_q8(x, w, residual=res, eps=eps)
+    check_rows(x, *got, w, res, eps)
+    for a, b in ((x.clone(), res), (x, res.clone())):
+        for c, d in zip(got, seq.rmsnorm_q8(a, w, residual=b, eps=eps, total=b if b is not res else a)):
+            assert torch.equal(c, d)
+    # weights that take the products back into the common range, or far above it
+    w = w * 1e30
+    check_rows(x, *seq.rmsnorm_q8(x, w, eps=eps), w, eps=eps)
+
+
 def test_rows_empty_and_refusals():
     z = torch.empty(0, 8, device="cuda")
     q, s, total = seq.rmsnorm_q8(z, torch.ones(8, device="cuda"), residual=z)
