@@ -355,7 +355,9 @@ int gconv_bwd_weight_noalloc(const gconv_desc *d, const void *x, const void *dy,
  * the states and their gradients are fp32, and the whole recurrence runs in
  * fp32 and rounds once, at each store.  A softplus(lambda) below fp32's normal
  * range (lambda under -87) counts as 0: the state is kept.  B and L may be 0.
- * lengths' values are clamped to [0, L] by the kernels. */
+ * lengths' values are clamped to [0, L] by the kernels.  An infinite h stays
+ * infinite while no infinity of the other sign enters and every a is in fp32's
+ * range; an a below it counts as 0, and makes such an h NaN. */
 typedef struct gconv_glr_desc {
     int32_t dtype;              /* gconv_dtype of x, r, i, y, dy, dx, dr, di */
     float c;                    /* finite, > 0 */

@@ -195,6 +195,38 @@ def test_recurrence_nan_stays_in_its_channel():
     assert bad[0, 100:, 5].all() and bad.sum() == 200 and torch.isnan(last).sum() == 1
 
 
+@pytest.mark.parametrize("t", list(TYPES))
+@pytest.mark.parametrize("B,L,D,split", [(1, 7, 8, True), (1, 100, 8, True), (2, 3000, 8, True), (2, 3000, 8, False)])
+def test_recurrence_infinite_values_stay(B, L, D, split, t):
+    """A state that is infinite stays so, however many steps a run or a chunk holds: products of their decays leave
+    fp32's range (a from e^-17 to e^-0.1 a step here), but no step's does.  The same for the gradient of the state."""
+    k = Case(B, L, D, t)
+    k.lam = torch.tensor([-5.0, -3, -1, 0, 0, 1, 2, 2]).cuda()
+    k.args = (k.x, k.r, k.i, k.lam)
+    none = None if split else torch.empty(0, dtype=torch.uint8, device="cuda")
+    plain, _, states = seq.glr_fwd(*k.args, h0=k.h0, save=True, workspace=none)
+    assert torch.isfinite(plain).all()
+    room = None if split else torch.empty(4 * B * D, dtype=torch.uint8, device="cuda")
+    inf = float("inf")
+    for at in sorted({0, 1, L // 3, L // 2, L - 1}):
+        k.dy[:, at, 1::2], k.dy[:, at, ::2] = inf, -inf
+        sign = torch.where(torch.arange(D, device="cuda") % 2 == 1, inf, -inf).expand(B, D)
+        dx, dr, di, dlam, dh0 = seq.glr_bwd(k.dy, *k.args, states, dh_last=k.dh, workspace=room)
+        assert torch.equal(dh0, sign), at
+        assert torch.equal(dx[:, :at + 1].float(), sign[:, None].expand(B, at + 1, D)), at
+        assert torch.isfinite(dx[:, at + 1:]).all()
+        k.dy[:, at] = 0
+        x = k.x.clone()
+        x[:, at, 1::2], x[:, at, ::2] = inf, -inf
+        y, last = seq.glr_fwd(x, *k.args[1:], h0=k.h0, workspace=none)
+        assert torch.equal(last, sign), at
+        assert torch.equal(y[:, :at], plain[:, :at]) and torch.equal(y[:, at:].float(), sign[:, None].expand(B, L - at, D)), at
+    y, last = seq.glr_fwd(*k.args, h0=torch.full_like(k.h0, inf), workspace=none)
+    assert (y == inf).all() and (last == inf).all()
+    dh0 = seq.glr_bwd(k.dy, *k.args, states, dh_last=torch.full_like(k.h0, -inf), workspace=room)[4]
+    assert (dh0 == -inf).all()
+
+
 @pytest.mark.parametrize("gate", ["r", "i"])
 def test_recurrence_nan_gate_reaches_its_gradient(gate):
     k = Case(1, 300, 32, "f32")
