@@ -249,7 +249,7 @@ __device__ __forceinline__ void publish(unsigned long long *to, float a, float h
     __hip_atomic_store(to, w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// The pair at `from` once it is there.  The wait is bounded (seconds, where
+// The pair at `from` once it is there.  The wait is bounded (about a second, where
 // it is microseconds in use) and ends in NaN.
 __device__ __forceinline__ float2 await(const unsigned long long *from)
 {

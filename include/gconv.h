@@ -381,9 +381,13 @@ int gconv_glr_fwd_workspace(const gconv_glr_desc *d, size_t *bytes);
 /* Forward.  h0 (NULL = zeros) and h_last (NULL = not wanted) are fp32
  * [B][D], packed, and may be the same memory.  lengths: int32 [B] in device
  * memory or NULL.  states: see GCONV_GLR_SPAN, or NULL.  workspace may be
- * NULL or smaller than the query's: the time axis is then not split.  No
- * atomics: the result is bitwise the same from run to run for one workspace
- * size. */
+ * NULL or smaller than the query's: the time axis is then not split.  The
+ * result is bitwise the same from run to run for one workspace size: where the
+ * time axis is split, chunks take their numbers from atomic counters, but what
+ * each computes goes by its number alone.  A chunk waits for those before it,
+ * all of which have begun by then; should the device stop running them for
+ * about a second, the wait ends and the row is NaN from that chunk on (the call,
+ * which has returned long before, reports nothing). */
 int gconv_glr_fwd(const gconv_glr_desc *d, const void *x, const void *r, const void *i,
                   const float *lambda, const float *h0, const int32_t *lengths, void *y,
                   float *h_last, float *states, void *workspace, size_t workspace_bytes,
