@@ -16,7 +16,7 @@ first call raises ``gconv.GconvUnavailable``.
 Activations need unit stride along their last axis; their other strides are
 free, so slices of a wider projection are taken as they are.  A call runs on
 the current stream of its tensors' device, or on ``stream`` (a hipStream_t as
-an int), and then its outputs and workspace are allocated for that stream.
+an int, 0 the default stream), and then its outputs and workspace are allocated for that stream.
 
 A call's arguments are checked once per set of sizes, strides, types and
 devices; the descriptor made then is kept under these (of an address, only
@@ -71,7 +71,9 @@ def _elsewhere(f, t, stream, *args, **kw):
     with torch.cuda.device(t.device):
         if stream is None:
             return f(*args, **kw)
-        with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=t.device)):
+        # 0 is the default stream's handle; ExternalStream takes it for a request for a new stream
+        on = torch.cuda.ExternalStream(stream, device=t.device) if stream else torch.cuda.default_stream(t.device)
+        with torch.cuda.stream(on):
             return f(*args, **kw)
 
 

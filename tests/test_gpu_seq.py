@@ -352,6 +352,38 @@ def test_recurrence_split_on_several_streams():
             assert all(torch.equal(a, b) for a, b in zip(w, want[j])) and all(torch.equal(a, b) for a, b in zip(g, back[j]))
 
 
+@pytest.mark.parametrize("handle", ["default", "own"])
+def test_stream_handles(handle):
+    """A call on a stream given by its handle, the default stream's 0 too, follows the work that is on it."""
+    own = torch.cuda.Stream() if handle == "own" else torch.cuda.default_stream()
+    k = Case(2, 300, 64, "f32")
+    a, sa, w, sw, bias = operands(20, 30, 64)
+    one = torch.ones(64, device="cuda")
+
+    def calls(stream):
+        q, s, total = seq.rmsnorm_q8(k.x[0], one, residual=k.dy[0], stream=stream)
+        y, last, states = seq.glr_fwd(*k.args, h0=k.h0, save=True, stream=stream)
+        grads = seq.glr_bwd(k.dy, *k.args, states, stream=stream)
+        step, _ = seq.glr_step(k.x[:, 0], k.r[:, 0], k.i[:, 0], k.lam, k.h0, h_out=torch.empty_like(k.h0), stream=stream)
+        return [q, s, total, *seq.quant_q8(k.x[0], stream=stream), y, last, *grads, step,
+                seq.matmul_q8(q, s, w, sw, stream=stream)]
+
+    x = k.x.clone()
+    want = calls(None)
+    torch.cuda.synchronize()
+    k.x.fill_(NAN)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(own):
+        torch.cuda._sleep(100_000_000)
+        k.x.copy_(x)
+    with torch.cuda.stream(torch.cuda.Stream()):   # the current stream is another one
+        got = calls(own.cuda_stream)
+    own.synchronize()
+    assert handle == "own" or own.cuda_stream == 0
+    for g, e in zip(got, want):
+        assert torch.equal(g, e)
+
+
 def test_recurrence_writes_only_its_places():
     """Outputs that are slices of wider tensors; what lies between stays."""
     B, L, D = 2, 130, 20
