@@ -32,7 +32,7 @@
 // is a queue: 1 x 16384 x 2048 80 us instead of 72, 1 x 4096 x 1024 18 instead
 // of 13.)  Backward, where P and Q come from r and dy alone, a kernel of its
 // own reduces every chunk first: its pairs handed on as in the forward pass,
-// 64 steps a block, 1 x 16384 x 2048 takes 182 us instead of 155.
+// 64 steps a block, 1 x 16384 x 2048 takes 182 us instead of 147.
 #include <type_traits>
 
 #include "device_common.h"
@@ -338,9 +338,9 @@ __device__ __forceinline__ float gather(const Params &p, int b, int ch, int orde
 
 // ------------------------------------------------------------- forward
 
-// 256 MB in and out take 66 us (1 x 16384 x 2048, split; 4.1 TB/s), of which the
+// 268 MB in and out take 64 us (1 x 16384 x 2048, split; 4.2 TB/s), of which the
 // same loads and stores alone, in 128-byte rows, take 54; the vector units are
-// busy 64% of the time.
+// busy 67% of the time.
 // SPLIT: a block takes one chunk of kFwdStep steps; else it walks its row's
 // whole time in such strides.  (Loads of a stride begun during the one before
 // gain nothing: 8 x 2048 x 2048 takes 75 us either way.)
@@ -554,8 +554,8 @@ template <typename T, bool FAR> __global__ __launch_bounds__(kLanes *kRuns) void
             (unsigned long long)__float_as_uint(at) << 32 | __float_as_uint(R);
 }
 
-// 8 x 2048 x 2048 takes 115 us, 4.1 TB/s of seven tensors, the vector units busy
-// 62% of the time.
+// 8 x 2048 x 2048 takes 113 us, 4.2 TB/s of seven tensors, the vector units busy
+// 65% of the time.
 // A block takes one chunk, the whole row where there is one.  AHEAD: it begins
 // a stride's loads while it works on the one before, in half as many registers
 // again: 134 -> 117 us for 8 x 2048 x 2048 (one block a compute unit), 101 ->

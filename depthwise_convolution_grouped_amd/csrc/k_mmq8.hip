@@ -116,8 +116,8 @@ template <typename T> __global__ __launch_bounds__(256) void any_k(Params p)
 // a lane fetches the piece that belongs at its place; the reads of one piece
 // from 16 consecutive rows then touch each of the 64 banks once.
 //
-// 8192 x 8192 x 4096 takes 250 us, 2.2 Pop/s, the matrix cores busy 62% of the
-// time; 8192 x 8192 x 8192 2.47 Pop/s.
+// 8192 x 8192 x 4096 takes 250 us, 2.2 Pop/s, the matrix cores busy 61% of the
+// cycles, of which there are 1.8 to the ns; 8192 x 8192 x 8192 2.5 Pop/s.
 
 typedef int i32x16 __attribute__((ext_vector_type(16)));
 typedef int rsrc_t __attribute__((ext_vector_type(4)));
@@ -561,7 +561,9 @@ __global__ __launch_bounds__(256) void pack_k(Pack q)
 }
 
 // The time of a tile shape in us, from its measured start and step (128 of k)
-// with one block a compute unit and with `side` of them side by side.
+// with one block a compute unit and with `side` of them side by side.  Only the
+// order of the shapes' times counts: on a full chip the clock goes down, and
+// 8192 x 8192 x 4096 takes 250 us where this says 190.
 double estimate(const Params &p, int bm, int bn, double start1, double step1, int side, double start2, double step2)
 {
     const double n = (double)up(p.M, bm) * up(p.N, bn), steps = (double)up(p.K, 128);
@@ -571,7 +573,7 @@ double estimate(const Params &p, int bm, int bn, double start1, double step1, in
 
 // Small tiles fill the chip, large ones read less: 2048 x 2048 x 2048 takes
 // 25.1 us with 256 x 256 tiles, 15.2 with 128 x 128 and 19.9 with 64 x 64;
-// 8192 x 8192 x 4096 takes 256, 315 and 448; 256 x 4096 x 4096 takes 41.1,
+// 8192 x 8192 x 4096 takes 250, 315 and 448; 256 x 4096 x 4096 takes 41.1,
 // 22.5 and 12.3.
 struct Times {
     double t256, t128, t64;
